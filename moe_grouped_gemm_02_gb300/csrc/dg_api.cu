@@ -515,9 +515,10 @@ dg_status run_gemm(const GemmCall& call, void* stream) {
     return e == cudaSuccess ? DG_OK : cuda_fail("kernel launch", e);
 }
 
+// rows: of A and D (per group); without any, their pointers may be null.
 dg_status check_common(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, const void* d,
-                       int N, int K) {
-    if (!a || !sfa || !b || !sfb || !d) return DG_ERR_INVALID_ARG;
+                       int N, int K, int rows = 1) {
+    if ((rows != 0 && (!a || !sfa || !d)) || !b || !sfb) return DG_ERR_INVALID_ARG;
     if (N <= 0 || K <= 0) return DG_ERR_INVALID_ARG;
     if (K % 128 != 0 || N % 8 != 0) return DG_ERR_SHAPE;
     if (!aligned16(a) || !aligned16(sfa) || !aligned16(b) || !aligned16(sfb) || !aligned16(d))
@@ -740,7 +741,7 @@ dg_status dg_fp8_gemm_nt_act(const void* a, const int32_t* sfa, const void* b, c
                              const void* residual, void* z, void* d, int M, int N, int K, int act, int bias_dtype,
                              void* stream) {
     if (M < 0) return DG_ERR_INVALID_ARG;
-    dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    dg_status s = check_common(a, sfa, b, sfb, d, N, K, M);
     if (s != DG_OK) return s;
     GemmCall call;
     if ((s = check_epilogue(call, bias, bias_dtype, residual, z, N, act)) != DG_OK) return s;
@@ -756,8 +757,8 @@ dg_status dg_m_grouped_fp8_gemm_nt_contiguous_act(const void* a, const int32_t* 
                                                   const void* bias, const void* residual, void* z, void* d,
                                                   const int32_t* m_indices, int M_sum, int N, int K, int G, int act,
                                                   int bias_dtype, void* stream) {
-    if (M_sum < 0 || G <= 0 || !m_indices) return DG_ERR_INVALID_ARG;
-    dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    if (M_sum < 0 || G <= 0 || (M_sum != 0 && !m_indices)) return DG_ERR_INVALID_ARG;
+    dg_status s = check_common(a, sfa, b, sfb, d, N, K, M_sum);
     if (s != DG_OK) return s;
     GemmCall call;
     if ((s = check_epilogue(call, bias, bias_dtype, residual, z, N, act)) != DG_OK) return s;
@@ -778,7 +779,7 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_act(const void* a, const int32_t* sfa,
                                               int bias_dtype, void* stream) {
     if (max_m < 0 || G <= 0 || !masked_m) return DG_ERR_INVALID_ARG;
     if (G > kMaxMaskedGroups) return DG_ERR_SHAPE;
-    dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    dg_status s = check_common(a, sfa, b, sfb, d, N, K, max_m);
     if (s != DG_OK) return s;
     GemmCall call;
     if ((s = check_epilogue(call, bias, bias_dtype, residual, z, N, act)) != DG_OK) return s;
@@ -795,7 +796,7 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_act(const void* a, const int32_t* sfa,
 dg_status dg_act_backward(const void* dd, const void* z, const int32_t* m_indices, void* dz, float* dbias,
                           float* workspace, int rows, int N, int G, int act, void* stream) {
     if ((rows != 0 && (!dd || !z || !dz)) || rows < 0 || N <= 0 || G <= 0 || act < ACT_NONE || act >= ACT_COUNT) return DG_ERR_INVALID_ARG;
-    if ((dbias && rows != 0 && !workspace) || (!m_indices && G != 1)) return DG_ERR_INVALID_ARG;
+    if (rows != 0 && ((dbias && !workspace) || (!m_indices && G != 1))) return DG_ERR_INVALID_ARG;
     if (N % (act == ACT_SWIGLU ? 16 : 8) != 0 || (m_indices && rows % 128 != 0) || G > kMaxMaskedGroups) return DG_ERR_SHAPE;
     if (!aligned16(dd) || !aligned16(z) || !aligned16(m_indices) || !aligned16(dz) || !aligned16(dbias) ||
         !aligned16(workspace))
