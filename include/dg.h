@@ -23,7 +23,8 @@
  *  - Every pointer is a DEVICE pointer owned by the caller.  The library allocates and frees
  *    no memory in any of these calls.
  *  - All tensors are dense and row-major (last dimension contiguous) with the shapes given.
- *  - Every pointer must be 16-byte aligned (TMA requirement), else DG_ERR_ALIGNMENT.
+ *  - Every pointer must be 16-byte aligned (TMA requirement), else DG_ERR_ALIGNMENT.  A pointer to
+ *    a tensor without elements (no tokens, no rows) may be NULL.
  *  - Calls are asynchronous on `stream` (a cudaStream_t passed as void*; NULL means the
  *    legacy default stream).  They never synchronize, except in validation mode (the
  *    environment variable DG_VALIDATE=1), where the device-side contracts below are read
@@ -250,8 +251,6 @@ dg_status dg_pack_sf_ue8m0(const float* sf, int32_t* out, int G, int MN, int K, 
  * Asynchronous on `stream`; buffers are the caller's; nothing is allocated.
  */
 dg_status dg_quantize_fp8_1x128(const void* x, void* q, int32_t* sf, int G, int M, int K, void* stream);
-
-/* In the calls below pointers to tensors without elements (no tokens, no rows) may be NULL. */
 
 /* Element types of the calls that take one, the router's scores, and the activations. */
 enum { DG_BF16 = 0, DG_F32 = 1 };

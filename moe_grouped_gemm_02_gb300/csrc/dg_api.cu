@@ -517,7 +517,7 @@ dg_status run_gemm(const GemmCall& call, void* stream) {
 
 // rows: of A and D (per group); without any, their pointers may be null.
 dg_status check_common(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, const void* d,
-                       int N, int K, int rows = 1) {
+                       int N, int K, int rows) {
     if ((rows != 0 && (!a || !sfa || !d)) || !b || !sfb) return DG_ERR_INVALID_ARG;
     if (N <= 0 || K <= 0) return DG_ERR_INVALID_ARG;
     if (K % 128 != 0 || N % 8 != 0) return DG_ERR_SHAPE;
@@ -589,7 +589,7 @@ extern "C" {
 dg_status dg_fp8_gemm_nt(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d, int M,
                          int N, int K, void* stream) {
     if (M < 0) return DG_ERR_INVALID_ARG;
-    const dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    const dg_status s = check_common(a, sfa, b, sfb, d, N, K, M);
     if (s != DG_OK) return s;
     if (static_cast<long long>(M) * K >= (1ll << 40) || static_cast<long long>(N) * K >= (1ll << 40))
         return DG_ERR_SHAPE;
@@ -603,8 +603,8 @@ dg_status dg_fp8_gemm_nt(const void* a, const int32_t* sfa, const void* b, const
 dg_status dg_m_grouped_fp8_gemm_nt_contiguous(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
                                               void* d, const int32_t* m_indices, int M_sum, int N, int K, int G,
                                               void* stream) {
-    if (M_sum < 0 || G <= 0 || !m_indices) return DG_ERR_INVALID_ARG;
-    const dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    if (M_sum < 0 || G <= 0 || (M_sum != 0 && !m_indices)) return DG_ERR_INVALID_ARG;
+    const dg_status s = check_common(a, sfa, b, sfb, d, N, K, M_sum);
     if (s != DG_OK) return s;
     if (M_sum % 128 != 0) return DG_ERR_SHAPE;
     if (static_cast<long long>(M_sum) * K >= (1ll << 40) || static_cast<long long>(G) * N * K >= (1ll << 40))
@@ -623,7 +623,7 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked(const void* a, const int32_t* sfa, con
                                           void* stream) {
     if (max_m < 0 || G <= 0 || !masked_m) return DG_ERR_INVALID_ARG;
     if (G > kMaxMaskedGroups) return DG_ERR_SHAPE;
-    const dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    const dg_status s = check_common(a, sfa, b, sfb, d, N, K, max_m);
     if (s != DG_OK) return s;
     if (static_cast<long long>(G) * max_m * K >= (1ll << 40) || static_cast<long long>(G) * N * K >= (1ll << 40))
         return DG_ERR_SHAPE;
@@ -639,7 +639,7 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked(const void* a, const int32_t* sfa, con
 dg_status dg_fp8_fp4_gemm_nt(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, void* d, int M,
                              int N, int K, void* stream) {
     if (M < 0) return DG_ERR_INVALID_ARG;
-    dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    dg_status s = check_common(a, sfa, b, sfb, d, N, K, M);
     if (s != DG_OK) return s;
     if ((s = check_fp4_b(b)) != DG_OK) return s;
     if (static_cast<long long>(M) * K >= (1ll << 40) || static_cast<long long>(N) * K >= (1ll << 40))
@@ -655,8 +655,8 @@ dg_status dg_fp8_fp4_gemm_nt(const void* a, const int32_t* sfa, const void* b, c
 dg_status dg_m_grouped_fp8_fp4_gemm_nt_contiguous(const void* a, const int32_t* sfa, const void* b,
                                                   const int32_t* sfb, void* d, const int32_t* m_indices, int M_sum,
                                                   int N, int K, int G, void* stream) {
-    if (M_sum < 0 || G <= 0 || !m_indices) return DG_ERR_INVALID_ARG;
-    dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    if (M_sum < 0 || G <= 0 || (M_sum != 0 && !m_indices)) return DG_ERR_INVALID_ARG;
+    dg_status s = check_common(a, sfa, b, sfb, d, N, K, M_sum);
     if (s != DG_OK) return s;
     if ((s = check_fp4_b(b)) != DG_OK) return s;
     if (M_sum % 128 != 0) return DG_ERR_SHAPE;
@@ -677,7 +677,7 @@ dg_status dg_m_grouped_fp8_fp4_gemm_nt_masked(const void* a, const int32_t* sfa,
                                               void* stream) {
     if (max_m < 0 || G <= 0 || !masked_m) return DG_ERR_INVALID_ARG;
     if (G > kMaxMaskedGroups) return DG_ERR_SHAPE;
-    dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    dg_status s = check_common(a, sfa, b, sfb, d, N, K, max_m);
     if (s != DG_OK) return s;
     if ((s = check_fp4_b(b)) != DG_OK) return s;
     if (static_cast<long long>(G) * max_m * K >= (1ll << 40) || static_cast<long long>(G) * N * K >= (1ll << 40))
@@ -697,7 +697,7 @@ dg_status dg_fp8_gemm(const void* a, const int32_t* sfa, const void* b, const in
     if (M < 0 || layout < DG_LAYOUT_NT || layout > DG_LAYOUT_TT || (out_f32 != 0 && out_f32 != 1))
         return DG_ERR_INVALID_ARG;
     if (c && !out_f32) return DG_ERR_INVALID_ARG;
-    const dg_status s = check_common(a, sfa, b, sfb, d, N, K);
+    const dg_status s = check_common(a, sfa, b, sfb, d, N, K, M);
     if (s != DG_OK) return s;
     if (c && !aligned16(c)) return DG_ERR_ALIGNMENT;
     const int a_mn = layout == DG_LAYOUT_TN || layout == DG_LAYOUT_TT;
@@ -717,7 +717,8 @@ dg_status dg_fp8_gemm(const void* a, const int32_t* sfa, const void* b, const in
 dg_status dg_k_grouped_fp8_gemm_tn_contiguous(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
                                               const float* c, float* d, const int32_t* ks, int G, int M, int N,
                                               int sum_K, void* stream) {
-    if (!a || !sfa || !b || !sfb || !d || !ks || G <= 0 || M < 0 || N <= 0 || sum_K < 0) return DG_ERR_INVALID_ARG;
+    if (!ks || G <= 0 || M < 0 || N <= 0 || sum_K < 0 || (M != 0 && !d)) return DG_ERR_INVALID_ARG;
+    if (sum_K != 0 && (!b || !sfb || (M != 0 && (!a || !sfa)))) return DG_ERR_INVALID_ARG;
     if (G > kMaxMaskedGroups) return DG_ERR_SHAPE;
     if (sum_K % 128 != 0 || M % 16 != 0 || N % 16 != 0) return DG_ERR_SHAPE;
     if (!aligned16(a) || !aligned16(sfa) || !aligned16(b) || !aligned16(sfb) || !aligned16(d) ||
@@ -732,7 +733,12 @@ dg_status dg_k_grouped_fp8_gemm_tn_contiguous(const void* a, const int32_t* sfa,
     call.a = a, call.sfa = sfa, call.b = b, call.sfb = sfb, call.d = d, call.c = c;
     call.out_f32 = 1, call.a_mn = 1, call.b_mn = 1;
     call.ks = ks;
-    // sum_K == 0: every group is empty and D = C (or zeros); the kernel still runs to write it.
+    // sum_K == 0: every group is empty and D = C (or zeros); the kernel still runs to write it.  It loads
+    // nothing, but the tensor maps need a base address: D's, where an operand without elements has none.
+    if (sum_K == 0) {
+        call.a = call.b = d;
+        call.sfa = call.sfb = reinterpret_cast<const int32_t*>(d);
+    }
     call.groups = G, call.rows = M, call.N = N, call.K = sum_K;
     return run_gemm(call, stream);
 }
@@ -931,7 +937,7 @@ dg_status dg_moe_combine_backward(const void* dy, const void* yp, const int32_t*
 
 dg_status dg_pack_sf_ue8m0(const float* sf, int32_t* out, int G, int MN, int K, int gran_mn, int gran_k,
                            void* stream) {
-    if (!sf || !out || G <= 0 || MN < 0 || K <= 0) return DG_ERR_INVALID_ARG;
+    if ((MN != 0 && (!sf || !out)) || G <= 0 || MN < 0 || K <= 0) return DG_ERR_INVALID_ARG;
     if (gran_mn != 1 && gran_mn != 128) return DG_ERR_INVALID_ARG;
     if (gran_k != 128) return DG_ERR_INVALID_ARG;
     if (K % 128 != 0) return DG_ERR_SHAPE;
@@ -949,7 +955,7 @@ dg_status dg_pack_sf_ue8m0(const float* sf, int32_t* out, int G, int MN, int K, 
 }
 
 dg_status dg_quantize_fp8_1x128(const void* x, void* q, int32_t* sf, int G, int M, int K, void* stream) {
-    if (!x || !q || !sf || G <= 0 || M < 0 || K <= 0) return DG_ERR_INVALID_ARG;
+    if ((M != 0 && (!x || !q || !sf)) || G <= 0 || M < 0 || K <= 0) return DG_ERR_INVALID_ARG;
     if (K % 128 != 0) return DG_ERR_SHAPE;
     if (!aligned16(x) || !aligned16(q) || !aligned16(sf)) return DG_ERR_ALIGNMENT;
     if (M == 0) return DG_OK;
@@ -963,12 +969,12 @@ dg_status dg_quantize_fp8_1x128(const void* x, void* q, int32_t* sf, int G, int 
 
 dg_status dg_pack_sf_ue8m0_k_grouped(const float* sf, int32_t* out, const int32_t* ks, int G, int MN, int sum_K,
                                      void* stream) {
-    if (!sf || !out || !ks || G <= 0 || MN < 0 || sum_K < 0) return DG_ERR_INVALID_ARG;
+    if (!ks || G <= 0 || MN < 0 || sum_K < 0 || (MN != 0 && sum_K != 0 && (!sf || !out))) return DG_ERR_INVALID_ARG;
     if (G > kMaxMaskedGroups || sum_K % 128 != 0) return DG_ERR_SHAPE;
     if (!aligned16(out) || (reinterpret_cast<uintptr_t>(sf) & 3u)) return DG_ERR_ALIGNMENT;
     const int kb_total = sum_K / 128;
     if (kb_total / 4 + G > 65535) return DG_ERR_SHAPE;
-    if (MN == 0) return DG_OK;
+    if (MN == 0 || sum_K == 0) return DG_OK;
     DeviceState* st = nullptr;
     const dg_status s = current_device(&st);
     if (s != DG_OK) return s;

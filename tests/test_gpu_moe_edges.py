@@ -45,3 +45,20 @@ def test_epilogues_without_rows(act):
                        m_indices=_empty(0, dtype=i32))
     dg.dg_check_device_error()
     assert torch.all(db == 0)
+
+
+def test_layer_without_tokens():
+    # forward and backward of the example layer on a rank without tokens: every weight's gradient is zeros
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_layer.py")
+    spec = importlib.util.spec_from_file_location("moe_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer = example.MoELayer(hidden=256, ffn=128, experts=3, choices=2)
+    x = _empty(0, 256)
+    y, kept = layer.forward(x)
+    grads = layer.backward(torch.empty_like(x), kept)
+    dg.dg_check_device_error()
+    assert y.shape == (0, 256) and grads.pop("x").shape == (0, 256)
+    assert set(grads) == {"router", "w1", "w2", "b1", "b2"} and all(torch.all(g == 0) for g in grads.values())

@@ -38,3 +38,25 @@ def test_activation_gradient_without_rows_takes_null(lib):
     for G in (1, 5):
         assert lib.dg_act_backward(None, None, None, None, None, None, 0, 256, G, 4, None) == OK
     assert lib.dg_act_backward(GOOD, GOOD, None, GOOD, None, None, 128, 256, 5, 4, None) == INVALID
+
+
+def test_other_calls_of_the_layer_without_rows_take_null(lib):
+    for b, want in ((GOOD, OK), (None, INVALID)):
+        assert lib.dg_fp8_gemm_nt(None, None, b, GOOD, None, 0, 512, 256, None) == want
+        assert lib.dg_m_grouped_fp8_gemm_nt_contiguous(None, None, b, GOOD, None, None, 0, 512, 256, 4, None) == want
+        assert lib.dg_m_grouped_fp8_gemm_nt_masked(None, None, b, GOOD, None, GOOD, 4, 0, 512, 256, None) == want
+        assert lib.dg_fp8_fp4_gemm_nt(None, None, b, GOOD, None, 0, 512, 256, None) == want
+        assert lib.dg_m_grouped_fp8_fp4_gemm_nt_contiguous(None, None, b, GOOD, None, None, 0, 512, 256, 4, None) == want
+        assert lib.dg_m_grouped_fp8_fp4_gemm_nt_masked(None, None, b, GOOD, None, GOOD, 4, 0, 512, 256, None) == want
+        assert lib.dg_fp8_gemm(None, None, b, GOOD, None, None, 0, 512, 256, 0, 0, None) == want
+    assert lib.dg_m_grouped_fp8_gemm_nt_contiguous(GOOD, GOOD, GOOD, GOOD, GOOD, None, 128, 512, 256, 4, None) == INVALID
+    assert lib.dg_quantize_fp8_1x128(None, None, None, 4, 0, 256, None) == OK
+    assert lib.dg_quantize_fp8_1x128(None, GOOD, GOOD, 1, 8, 256, None) == INVALID
+    assert lib.dg_pack_sf_ue8m0(None, None, 1, 0, 256, 1, 128, None) == OK
+    assert lib.dg_pack_sf_ue8m0_k_grouped(None, None, GOOD, 4, 64, 0, None) == OK
+    assert lib.dg_pack_sf_ue8m0_k_grouped(None, GOOD, GOOD, 4, 64, 128, None) == INVALID
+    k = lib.dg_k_grouped_fp8_gemm_tn_contiguous
+    assert k(None, None, None, None, None, None, GOOD, 4, 0, 64, 0, None) == OK           # no columns of A either
+    for hole in range(5):
+        a, sfa, b, sfb, d = (None if i == hole else GOOD for i in range(5))
+        assert k(a, sfa, b, sfb, None, d, GOOD, 4, 64, 64, 128, None) == INVALID
