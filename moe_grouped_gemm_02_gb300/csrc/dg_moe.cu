@@ -364,8 +364,14 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, off));
     m = fmaxf(m, -FLT_MAX);      // (a row with nothing available: every term below is 0)
     float s = 0.0f, slope = 1.0f, sum = 0.0f;
-    if (my_i >= 0) s = sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - m);
-    if (sigmoid) slope = 1.0f - s;
+    if (sigmoid) {
+        // both from e^-|x|: 1 - s of a rounded s would lose the slope of a large logit (all of it from 17 on)
+        const float e = expf(-fabsf(x)), r = 1.0f / (1.0f + e);
+        s = my_i < 0 ? 0.0f : x >= 0.0f ? r : e * r;
+        slope = x >= 0.0f ? e * r : r;
+    } else if (my_i >= 0) {
+        s = expf(x - m);
+    }
     if (all) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {

@@ -62,3 +62,50 @@ def test_layer_without_tokens():
     dg.dg_check_device_error()
     assert y.shape == (0, 256) and grads.pop("x").shape == (0, 256)
     assert set(grads) == {"router", "w1", "w2", "b1", "b2"} and all(torch.all(g == 0) for g in grads.values())
+
+
+# ---------------------------------------------------------------------------------------------
+# Router: extreme logits
+# ---------------------------------------------------------------------------------------------
+EPS = 2.0 ** -24
+
+
+def _sigmoid(x):
+    # in 64 bits, to a few of their units at either end
+    e = np.exp(-np.abs(x))
+    return np.where(x >= 0, 1 / (1 + e), e / (1 + e))
+
+
+def _as(x, dtype):
+    t = torch.from_numpy(np.asarray(x, dtype=np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    return t.cuda(), t.double().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_slope_of_large_logits(dtype, renorm):
+    # dl_c = scale q_c (1 - s_c) (dw_c - mean): the slope 1 - s is e^-x for a large logit x.  A score or a slope
+    # is an exponential (2 units), a sum, a quotient and a product; q one quotient and two sums over k more: below
+    # 64 eps of q (1 - s) (|dw| + sum |dw q|), BF16 logits' gradients rounded once more
+    T, E, k = 48, 16, 8
+    r = _rng(31)
+    x = r.uniform(8, 30, (T, E)) * np.where(r.random((T, E)) < 0.25, -1, 1)
+    x[:, 0] = r.uniform(-2, 2, T)
+    x, xv = _as(x, dtype)
+    idx, w = _empty(T, k, dtype=torch.int32), _empty(T, k, dtype=torch.float32)
+    dg.dg_moe_route(x, idx, w, scoring="sigmoid", renormalize=renorm, scale=2.5)
+    dw = r.standard_normal((T, k)).astype(np.float32)
+    dl = torch.full((T, E), 7.0, dtype=x.dtype, device="cuda")
+    dg.dg_moe_route_backward(x, idx, to_dev(dw), dl, scoring="sigmoid", renormalize=renorm, scale=2.5)
+    at = idx.long().cpu().numpy()
+    chosen = np.take_along_axis(xv, at, 1)
+    s, slope, g = _sigmoid(chosen), _sigmoid(-chosen), dw.astype(np.float64)
+    q = s / s.sum(1, keepdims=True) if renorm else s
+    mean = (g * q).sum(1, keepdims=True) if renorm else 0.0
+    size = np.abs(g) + (np.abs(g * q).sum(1, keepdims=True) if renorm else 0.0)
+    want, bound = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(want, at, 2.5 * q * slope * (g - mean), 1)
+    np.put_along_axis(bound, at, 64 * EPS * 2.5 * q * slope * size, 1)
+    if dtype == "bf16":
+        bound += 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(dl.double().cpu().numpy() - want) <= bound)
