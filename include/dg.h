@@ -312,7 +312,8 @@ dg_status dg_act_backward(const void* dd, const void* z, const int32_t* m_indice
  *             -1 where fewer than k experts are open
  *   topk_w    FP32 [T][k]: scale * score, 0 where topk_idx is -1
  * score: DG_SCORE_SOFTMAX, the softmax over the token's E logits; DG_SCORE_SIGMOID, the logit's
- * sigmoid.  renormalize = 1 divides by the sum over the chosen (0 where that sum is 0).
+ * sigmoid (0 for logits below -700: masks of large negative values).  renormalize = 1 divides by the
+ * sum over the chosen (0 where that sum is 0), also where the scores are too small for FP32.
  * Requires 1 <= k <= 32, k <= E <= 1024, T >= 0 (0 is a no-op).
  *
  * dg_moe_route_backward: dlogits [T][E] (the logits' type, fully overwritten) from dw [T][k], the

@@ -179,6 +179,15 @@ __device__ __forceinline__ void sort_descending(uint32_t (&e)[N]) {
                     }
 }
 
+// sigmoid(x) e^-min(top, 0), x <= top: the sigmoid itself with top = 0.  With a token's largest chosen logit as
+// top the scores' sum is at least 1/2 and their ratios stay right where the scores themselves underflow (logits
+// below about -87).  A logit below SIGMOID_ZERO, such as a mask of the type's lowest value, scores 0.
+constexpr float SIGMOID_ZERO = -700.0f;
+__device__ __forceinline__ float sigmoid_over(float x, float top) {
+    const float up = x >= 0.0f ? 1.0f : x >= SIGMOID_ZERO ? expf(x - fminf(top, 0.0f)) : 0.0f;
+    return __fdividef(up, 1.0f + expf(-fabsf(x)));
+}
+
 // group: tokens whose choices share the lanes of the last steps (scores, sums, stores), each
 // with slot lanes (a power of two >= k).
 // (12 CTAs per SM leave 40 registers: at the compiler's own choice of 31, 32768 x 256 BF16 took 11.1 us, now 10.2.)
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV <= 8 ? 12 : 0)
     }
     const float top = __shfl_sync(FULL, value, my_slot * slot);
     float w = 0.0f;
-    if (have) w = sigmoid ? __fdividef(1.0f, 1.0f + expf(-value)) : expf(value - top);
+    if (have) w = sigmoid ? sigmoid_over(value, renorm ? top : 0.0f) : expf(value - top);
     if (renorm) {
         sum = w;
 #pragma unroll
@@ -367,7 +376,8 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS)
     if (sigmoid) {
         // both from e^-|x|: 1 - s of a rounded s would lose the slope of a large logit (all of it from 17 on)
         const float e = expf(-fabsf(x)), r = 1.0f / (1.0f + e);
-        s = my_i < 0 ? 0.0f : x >= 0.0f ? r : e * r;
+        // (as sigmoid_over; x is -inf where there is no choice)
+        s = x >= 0.0f ? r : x >= SIGMOID_ZERO ? (renorm ? expf(x - fminf(m, 0.0f)) : e) * r : 0.0f;
         slope = x >= 0.0f ? e * r : r;
     } else if (my_i >= 0) {
         s = expf(x - m);

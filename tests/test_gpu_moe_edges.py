@@ -109,3 +109,38 @@ def test_sigmoid_slope_of_large_logits(dtype, renorm):
     if dtype == "bf16":
         bound += 2.0 ** -8 * np.abs(want)
     assert np.all(np.abs(dl.double().cpu().numpy() - want) <= bound)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_renormalised_sigmoid_of_scores_that_underflow(dtype):
+    # every chosen logit so far below zero that its sigmoid has no FP32 value: the weights are the scores'
+    # ratios all the same (down to logits of -700: below, masks, the scores are 0).  Differences of logits are rounded to 2^-22 at most (spread 8: 4 eps of the
+    # exponential); with the rest of the arithmetic as above, 64 eps
+    k, E = 6, 16
+    r = _rng(41)
+    centre = np.repeat([-87.5, -88.5, -95.0, -104.0, -200.0, -1e4, -3e38], 5)[:, None]
+    x = centre + r.uniform(-8, 0, (35, E))
+    x = np.concatenate([x, np.where(np.arange(E) == 3, 3.0, -95.0)[None] + r.uniform(-1, 0, (1, E))])   # one large, the rest far below
+    x, xv = _as(x, dtype)
+    T = xv.shape[0]
+    idx, w = _empty(T, k, dtype=torch.int32), _empty(T, k, dtype=torch.float32)
+    dg.dg_moe_route(x, idx, w, scoring="sigmoid", renormalize=True, scale=2.5)
+    at = np.argsort(-xv, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(idx.cpu().numpy(), at)
+    chosen = np.take_along_axis(xv, at, 1)
+    top = np.minimum(chosen[:, :1], 0)
+    s = np.where(chosen >= 0, 1.0, np.exp(np.minimum(chosen - top, 0))) / (1 + np.exp(-np.abs(chosen)))
+    s[chosen < -700] = 0
+    q = s / np.maximum(s.sum(1, keepdims=True), 1e-300)
+    tiny = 2.0 ** -145                           # (the last row's small scores are subnormal)
+    assert np.all(np.abs(w.double().cpu().numpy() - 2.5 * q) <= 64 * EPS * 2.5 * q + tiny)
+    dw = r.standard_normal((T, k)).astype(np.float32)
+    dl = torch.full((T, E), 7.0, dtype=x.dtype, device="cuda")
+    dg.dg_moe_route_backward(x, idx, to_dev(dw), dl, scoring="sigmoid", renormalize=True, scale=2.5)
+    g, slope = dw.astype(np.float64), _sigmoid(-chosen)
+    want, bound = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(want, at, 2.5 * q * slope * (g - (g * q).sum(1, keepdims=True)), 1)
+    np.put_along_axis(bound, at, 64 * EPS * 2.5 * q * slope * (np.abs(g) + np.abs(g * q).sum(1, keepdims=True)), 1)
+    if dtype == "bf16":
+        bound += 2.0 ** -8 * np.abs(want) + 2.0 ** -134      # BF16's subnormals are 2^-133 apart
+    assert np.all(np.abs(dl.double().cpu().numpy() - want) <= bound + 4 * tiny)
