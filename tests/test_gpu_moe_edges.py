@@ -144,3 +144,18 @@ def test_renormalised_sigmoid_of_scores_that_underflow(dtype):
     if dtype == "bf16":
         bound += 2.0 ** -8 * np.abs(want) + 2.0 ** -134      # BF16's subnormals are 2^-133 apart
     assert np.all(np.abs(dl.double().cpu().numpy() - want) <= bound + 4 * tiny)
+
+
+def test_weights_of_equal_logits_are_rounded_once():
+    # equal logits: every exponential is exactly 1 and their sum an integer, so the weight is 1 / n, rounded to
+    # the nearest FP32 value by the one division
+    for E in list(range(1, 400)) + [512, 513, 777, 1000, 1021, 1024]:
+        for dtype in (torch.float32, torch.bfloat16):
+            x = torch.full((2, E), 0.75, dtype=dtype, device="cuda")
+            for k, scoring, renorm, n in ((1, "softmax", False, E), (min(E, 31), "softmax", True, min(E, 31)),
+                                          (min(E, 27), "sigmoid", True, min(E, 27))):
+                if scoring == "sigmoid":
+                    x.zero_()                                          # scores of exactly 1/2
+                idx, w = _empty(2, k, dtype=torch.int32), _empty(2, k, dtype=torch.float32)
+                dg.dg_moe_route(x, idx, w, scoring=scoring, renormalize=renorm)
+                assert np.all(w.cpu().numpy() == np.float32(1) / np.float32(n)), (E, dtype, scoring, renorm)
