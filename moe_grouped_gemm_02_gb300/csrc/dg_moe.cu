@@ -161,22 +161,22 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ uint32_t bf16_key(uint32_t m) { return (m & 0xFFFF0000u) | ((m >> 31) ? 0u : 0xFFFFu); }
 constexpr uint32_t KEY_NONE = 0x007FFFFFu;   // order_key(-inf): nothing at or below it is chosen
 
-// Batcher's odd-even merge sort of N (a power of two) keys, descending.
-template <int N>
+// Batcher's odd-even merge sort of N (a power of two) keys, descending: for P = 1, 2, .., N / 2 and Q = P, P / 2,
+// .., 1 the exchanges of keys Q apart.  The steps are template parameters and each is one flat loop, so that every
+// index is a constant and the keys stay in registers (as nested loops they went to local memory at N = 32).
+template <int N, int P = 1, int Q = 1>
 __device__ __forceinline__ void sort_descending(uint32_t (&e)[N]) {
+    if constexpr (P < N) {
 #pragma unroll
-    for (int p = 1; p < N; p *= 2)
-#pragma unroll
-        for (int q = p; q >= 1; q /= 2)
-#pragma unroll
-            for (int j = q % p; j + q < N; j += 2 * q)
-#pragma unroll
-                for (int i = 0; i < q; ++i)
-                    if (j + i + q < N && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
-                        const uint32_t a = e[j + i], b = e[j + i + q];
-                        e[j + i] = max(a, b);
-                        e[j + i + q] = min(a, b);
-                    }
+        for (int i = Q % P; i + Q < N; ++i)
+            if ((i - Q % P) % (2 * Q) < Q && i / (2 * P) == (i + Q) / (2 * P)) {
+                const uint32_t a = e[i], b = e[i + Q];
+                e[i] = max(a, b);
+                e[i + Q] = min(a, b);
+            }
+        if constexpr (Q > 1) sort_descending<N, P, Q / 2>(e);
+        else sort_descending<N, 2 * P, 2 * P>(e);
+    }
 }
 
 // a / b, 0 <= a <= b, b from 1/2 to 1024 (or a = 0): a quotient good to two units and one step of correction by its

@@ -1,6 +1,9 @@
 """CPU checks of the MoE operators' calls at the edges of their contracts: what they accept and refuse
 before anything is launched."""
 import ctypes
+import os
+import re
+import subprocess
 
 import pytest
 
@@ -60,3 +63,16 @@ def test_other_calls_of_the_layer_without_rows_take_null(lib):
     for hole in range(5):
         a, sfa, b, sfb, d = (None if i == hole else GOOD for i in range(5))
         assert k(a, sfa, b, sfb, None, d, GOOD, 4, 64, 64, 128, None) == INVALID
+
+
+@pytest.mark.parametrize("source", ["dg_moe.cu", "dg_act.cu", "dg_quant.cu", "dg_pack.cu"])
+def test_kernels_use_no_local_memory(source, tmp_path):
+    # the compiler's report: no stack frame (an array indexed at run time) and no spilled registers
+    cmd = [dg_build._nvcc(), *dg_build.GENCODE, *dg_build.FLAGS, "-Xptxas", "-v", "-c", os.path.join(dg_build.CSRC, source),
+           "-o", str(tmp_path / "out.o")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    kernels = re.findall(r"Function properties for (\S+)\s+(\d+) bytes stack frame, (\d+) bytes spill stores, (\d+) bytes spill loads",
+                         r.stdout + r.stderr)
+    assert kernels
+    assert [k for k in kernels if k[1:] != ("0", "0", "0")] == []
