@@ -294,8 +294,8 @@ def packed_sf_shape(groups: int | None, mn: int, K: int) -> tuple:
 
 # ---------------------------------------------------------------------------------------------
 # MoE operators around the GEMMs.  Their sizes come from several tensors: the compiled binding
-# (csrc/dg_binding.cpp) checks that types and shapes agree, raising TypeError or ValueError, before
-# a pointer reaches the library.
+# (csrc/dg_binding.cpp) checks that types and shapes agree and that every tensor is on the current
+# device, raising TypeError or ValueError, before a pointer reaches the library.
 # ---------------------------------------------------------------------------------------------
 _binding = None
 

@@ -5,11 +5,13 @@
 //
 // Every function takes its tensors first, then plain numbers, then the stream (an address, or
 // None for torch's current one), and returns the call's status.  A tensor of a wrong type or
-// shape raises TypeError or ValueError before anything is called.
+// shape, or of another device than the current one, raises TypeError or ValueError before anything is
+// called.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -53,10 +55,16 @@ struct Raised {};
     throw Raised();
 }
 
+// The current device, as the call under way found it (-1: not asked yet).
+thread_local int call_device = -1;
+
 const at::Tensor& tensor(PyObject* o, const char* what) {
     if (!THPVariable_Check(o)) raise(PyExc_TypeError, what, "be a CUDA tensor");
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) raise(PyExc_TypeError, what, "be a CUDA tensor");
+    if (call_device < 0) call_device = c10::cuda::current_device();
+    // (the launch goes to the current device, whose kernels may not read another's memory)
+    if (t.get_device() != call_device) raise(PyExc_ValueError, what, "be on the current CUDA device");
     if (!t.is_contiguous()) raise(PyExc_ValueError, what, "be contiguous");
     return t;
 }
@@ -137,6 +145,7 @@ PyObject* guarded(Py_ssize_t n, const F& f) {
         return nullptr;
     }
     try {
+        call_device = -1;
         return PyLong_FromLong(f());
     } catch (const Raised&) {
     } catch (const std::exception& e) {

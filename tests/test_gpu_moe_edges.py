@@ -159,3 +159,28 @@ def test_weights_of_equal_logits_are_rounded_once():
                 idx, w = _empty(2, k, dtype=torch.int32), _empty(2, k, dtype=torch.float32)
                 dg.dg_moe_route(x, idx, w, scoring=scoring, renormalize=renorm)
                 assert np.all(w.cpu().numpy() == np.float32(1) / np.float32(n)), (E, dtype, scoring, renorm)
+
+
+# ---------------------------------------------------------------------------------------------
+# Tensors of another device
+# ---------------------------------------------------------------------------------------------
+def test_tensors_of_another_device_are_refused():
+    # (tensors with a null pointer stand for those of a second GPU: nothing could be launched on them)
+    class Far(torch.Tensor):
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise AssertionError(f"{func} of a tensor without memory")
+
+    def far_tensor(shape, dtype):
+        return torch.Tensor._make_wrapper_subclass(Far, shape, dtype=dtype, device=torch.device("cuda", 1))
+
+    far, far_logits, far_w = far_tensor((4, 2), torch.int32), far_tensor((4, 8), torch.float32), far_tensor((4, 2), torch.float32)
+    assert far.device.index == 1 and torch.cuda.current_device() == 0
+    here = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    n = torch.zeros((4,), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="current CUDA device"):
+        dg.dg_moe_sort_masked(far, here, n, 8)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        dg.dg_moe_sort_masked(here, far, n, 8)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        dg.dg_moe_route(far_logits, far, far_w)

@@ -76,3 +76,13 @@ def test_kernels_use_no_local_memory(source, tmp_path):
                          r.stdout + r.stderr)
     assert kernels
     assert [k for k in kernels if k[1:] != ("0", "0", "0")] == []
+
+
+def test_host_tensors_are_refused():
+    torch = pytest.importorskip("torch")
+    dg_build.build()
+    idx = torch.zeros((4, 2), dtype=torch.int32)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        dg.dg_moe_sort_masked(idx, idx, idx[:, 0].contiguous(), 8)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        dg.dg_act_backward(idx, idx, idx)
