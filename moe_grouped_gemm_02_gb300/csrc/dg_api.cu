@@ -31,6 +31,7 @@ struct DeviceState {
     int* err_ptr = nullptr;
     int max_smem = 0;   // opt-in dynamic shared memory per block
     bool prepared = false;
+    int sort_cluster = 0;   // CTAs of the token sort's cluster
     int clusters[16][7] = {};   // co-resident clusters per configuration and split 2..8 (0: unknown)
 };
 
@@ -117,7 +118,7 @@ dg_status current_device(DeviceState** out) {
         const KernelConfig* const* cfgs = all_configs(&n);
         for (int i = 0; i < n; ++i)
             if ((e = cfgs[i]->prepare(st.max_smem)) != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
-        if ((e = prepare_moe(st.max_smem)) != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
+        if ((e = prepare_moe(st.max_smem, &st.sort_cluster)) != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
         st.prepared = true;
     }
     *out = &st;
@@ -574,8 +575,8 @@ dg_status run_sort(const int32_t* topk_idx, int32_t* pos, int32_t* m_indices, in
     DeviceState* st = nullptr;
     const dg_status s = current_device(&st);
     if (s != DG_OK) return s;
-    const cudaError_t e = launch_moe_sort(topk_idx, pos, m_indices, counts, ks, T * k, G, rows, max_m, pdl_enabled(),
-                                          static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_moe_sort(topk_idx, pos, m_indices, counts, ks, T * k, G, rows, max_m, st->sort_cluster,
+                                          pdl_enabled(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DG_OK : cuda_fail("dg_moe_sort", e);
 }
 

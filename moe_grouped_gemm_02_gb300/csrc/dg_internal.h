@@ -106,14 +106,14 @@ cudaError_t launch_pack_sf(const float* sf, int32_t* out, int G, int MN, int MNb
                            int mn_al, int gran_mn, int pdl, cudaStream_t stream);
 cudaError_t launch_pack_sf_k_grouped(const float* sf, int32_t* out, const int32_t* ks, int G, int MN, int mn_al,
                                      int kb_total, int pdl, cudaStream_t stream);
-cudaError_t prepare_moe(int max_smem);
+cudaError_t prepare_moe(int max_smem, int* sort_cluster);
 cudaError_t launch_moe_route(const void* logits, int32_t* topk_idx, float* topk_w, int T, int E, int k, int f32,
                              int sigmoid, int renorm, float scale, int pdl, cudaStream_t stream);
 cudaError_t launch_moe_route_backward(const void* logits, const int32_t* topk_idx, const float* dw, void* dlogits,
                                       int T, int E, int k, int f32, int sigmoid, int renorm, float scale, int pdl,
                                       cudaStream_t stream);
 cudaError_t launch_moe_sort(const int32_t* idx, int32_t* pos, int32_t* m_indices, int32_t* counts, int32_t* ks, int n,
-                            int G, int rows, int max_m, int pdl, cudaStream_t stream);
+                            int G, int rows, int max_m, int cluster, int pdl, cudaStream_t stream);
 cudaError_t launch_moe_dispatch_fp8(const void* x, const int32_t* pos, const int32_t* m_indices, void* q, int32_t* sf,
                                     int T, int k, int K, int G, int rows, int pdl, cudaStream_t stream);
 cudaError_t launch_moe_dispatch(const void* x, const int32_t* pos, const int32_t* m_indices, void* out, int T, int k,

@@ -1023,10 +1023,6 @@ cudaError_t launch_moe_route_backward(const void* logits, const int32_t* topk_id
     return f32 ? go(route_backward_kernel<32, true>) : go(route_backward_kernel<32, false>);
 }
 
-// CTAs of the sort's cluster: 16 where the GPU takes clusters beyond the portable size, else 8.
-static int g_sort_cluster = 0;
-static int sort_cluster() { return g_sort_cluster; }
-
 // f(kernel) of the sort kernel for G experts: the bits of an expert's index, rounded up to 4, 6, 8 or 12.
 template <bool CLUSTER, class F>
 static cudaError_t with_sort_kernel(int G, const F& f) {
@@ -1036,7 +1032,8 @@ static cudaError_t with_sort_kernel(int G, const F& f) {
     return f(sort_kernel<CLUSTER, 12>);
 }
 
-cudaError_t prepare_moe(int max_smem) {
+// *sort_cluster: CTAs of the sort's cluster on this device, 16 where it takes clusters beyond the portable size, else 8.
+cudaError_t prepare_moe(int max_smem, int* sort_cluster) {
     auto smem = [&](auto kernel) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
     };
@@ -1060,18 +1057,18 @@ cudaError_t prepare_moe(int max_smem) {
     cfg.numAttrs = 1;
     int clusters = 0;
     if (cudaOccupancyMaxActiveClusters(&clusters, sort_kernel<true, 12>, &cfg) != cudaSuccess) cudaGetLastError();
-    g_sort_cluster = clusters > 0 ? 16 : 8;
+    *sort_cluster = clusters > 0 ? 16 : 8;
     return cudaSuccess;
 }
 
 cudaError_t launch_moe_sort(const int32_t* idx, int32_t* pos, int32_t* m_indices, int32_t* counts, int32_t* ks, int n,
-                            int G, int rows, int max_m, int pdl, cudaStream_t stream) {
+                            int G, int rows, int max_m, int cluster, int pdl, cudaStream_t stream) {
     SortArgs a{idx, pos, m_indices, counts, ks, n, G, rows, max_m, 0};
     const int warps = sort_warps(G);
     // One CTA for decode batches, else a cluster.  Measured (us, one CTA / cluster of 16): 64 experts, 512
     // slots 4.1 / 4.2, 2048 slots 5.2 / 4.9, 16384 slots 13.7 / 4.9, 262144 slots 163 / 14.7; 256 experts (33024
     // rows to fill) 512 slots 7.7 / 4.9.
-    const int ctas = n <= 1024 && rows <= 10240 ? 1 : sort_cluster();
+    const int ctas = n <= 1024 && rows <= 10240 ? 1 : cluster;
     const long long per = (static_cast<long long>(n) + ctas * warps - 1) / (ctas * warps);
     a.share = static_cast<int>((per + 31) / 32 * 32);
     cudaLaunchConfig_t cfg = {};

@@ -86,3 +86,14 @@ def test_host_tensors_are_refused():
         dg.dg_moe_sort_masked(idx, idx, idx[:, 0].contiguous(), 8)
     with pytest.raises(TypeError, match="CUDA tensor"):
         dg.dg_act_backward(idx, idx, idx)
+
+
+def test_launchers_keep_no_state_between_calls():
+    # what belongs to a device is in the device's state (dg_api.cu), under its lock: the files with the kernels and their
+    # launches have no variable of their own
+    for name in sorted(os.listdir(dg_build.CSRC)):
+        if name == "dg_api.cu" or not name.endswith((".cu", ".cuh")):
+            continue
+        text = open(os.path.join(dg_build.CSRC, name)).read()
+        found = re.findall(r"^(?:static |inline |__device__ )*[\w:]+ \**g_\w+ *(?:=|;|\[).*$", text, re.M)
+        assert found == [], name
