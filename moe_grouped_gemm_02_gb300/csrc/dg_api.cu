@@ -31,6 +31,7 @@ struct DeviceState {
     int* err_ptr = nullptr;
     int max_smem = 0;   // opt-in dynamic shared memory per block
     bool prepared = false;
+    bool act_prepared[16] = {};   // per configuration: its epilogue kernels
     int sort_cluster = 0;   // CTAs of the token sort's cluster
     int clusters[16][7] = {};   // co-resident clusters per configuration and split 2..8 (0: unknown)
 };
@@ -125,6 +126,16 @@ dg_status current_device(DeviceState** out) {
     return DG_OK;
 }
 
+// The attributes of a configuration's epilogue kernels, set on the first call that uses them: setting them loads
+// the kernels, ten to thirty of a configuration, which the plain GEMMs need not wait for or hold in memory.
+cudaError_t prepare_epilogue(DeviceState& st, const KernelConfig* c, int index) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (st.act_prepared[index]) return cudaSuccess;
+    const cudaError_t e = c->prepare_act(st.max_smem);
+    st.act_prepared[index] = e == cudaSuccess;
+    return e;
+}
+
 int effective_sms(const DeviceState& st) {
     std::lock_guard<std::mutex> lk(g_mu);
     const int cap = sms_cap_locked();
@@ -170,6 +181,7 @@ bool encode_3d(CUtensorMap* m, CUtensorMapDataType dt, uint64_t elem_bytes, cons
 // co-resident CTA or cluster.
 struct Plan {
     const KernelConfig* cfg = nullptr;
+    int index = 0;      // of the configuration
     int split = 1;
     int capacity = 0;   // co-resident CTAs (plain) or clusters (split > 1)
     int tma_store = 0;  // room for the epilogue's output staging buffers
@@ -261,6 +273,7 @@ Plan choose_plan(DeviceState& st, int mode, int rows, int m_blocks_total, int N,
                                 (cost < best_cost - 1e-9 && c->ks >= best.cfg->ks);
             if (better) {
                 best.cfg = c;
+                best.index = i;
                 best.split = split;
                 best.capacity = cap;
                 best.tma_store = tma_store;
@@ -380,6 +393,10 @@ dg_status run_gemm(const GemmCall& call, void* stream) {
                                   call.b_mn, call.b_fp4, call.epilogue, hbm_bytes);
     if (!plan.cfg) return DG_ERR_SHAPE;   // nothing fits in shared memory (too many groups)
     const KernelConfig* cfg = plan.cfg;
+    if (call.epilogue) {
+        const cudaError_t e = prepare_epilogue(*st, cfg, plan.index);
+        if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
+    }
 
     CUtensorMap maps[6];
     // A and D have one group per masked group; B one per expert (contiguous, masked).  K-grouped

@@ -2012,8 +2012,7 @@ cudaError_t prepare_fp8_gemm(int max_smem) {
 template <class C>
 cudaError_t prepare_fp8_gemm_act(int max_smem) {
     auto prep = [&](auto kernel) { return prepare_kernel<C>(kernel, max_smem); };
-    cudaError_t e = prepare_fp8_gemm<C>(max_smem);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     auto all = [&](auto spec) {
         constexpr int S = decltype(spec)::value;
         constexpr int H = C::ACC_ROT == 1 ? ACT_COUNT : 0, D = C::MH == 2 ? ACT_COUNT : 0;
@@ -2036,15 +2035,15 @@ cudaError_t prepare_fp8_gemm_act(int max_smem) {
     return all(std::integral_constant<int, V ? SPEC_MASKED : SPEC_ANY>());
 }
 
-#define DG_DEFINE_CONFIG_FN(FN, BN_, ST_, AC_, MH_, KS_, AR_, ACTFN_, ACTSMEM_, PREPFN_)                              \
+#define DG_DEFINE_CONFIG_FN(FN, BN_, ST_, AC_, MH_, KS_, AR_, ACTFN_, ACTSMEM_, ACTPREP_)                             \
     const KernelConfig& FN() {                                                                             \
         using C = GemmCfg<BN_, ST_, AC_, MH_, KS_, AR_>;                                                   \
         static const KernelConfig cfg{BN_, ST_, AC_, MH_, KS_, AR_, #FN, &C::smem_bytes, &launch_fp8_gemm<C>, \
-                                      ACTFN_, ACTSMEM_, PREPFN_, &max_clusters_fp8_gemm<C>};                         \
+                                      ACTFN_, ACTSMEM_, &prepare_fp8_gemm<C>, ACTPREP_, &max_clusters_fp8_gemm<C>};  \
         return cfg;                                                                                        \
     }
 #define DG_DEFINE_CONFIG_AR(FN, BN_, ST_, AC_, MH_, KS_, AR_) \
-    DG_DEFINE_CONFIG_FN(FN, BN_, ST_, AC_, MH_, KS_, AR_, nullptr, nullptr, &prepare_fp8_gemm<C>)
+    DG_DEFINE_CONFIG_FN(FN, BN_, ST_, AC_, MH_, KS_, AR_, nullptr, nullptr, nullptr)
 #define DG_DEFINE_CONFIG_KS(FN, BN_, ST_, AC_, MH_, KS_) DG_DEFINE_CONFIG_AR(FN, BN_, ST_, AC_, MH_, KS_, 128)
 #define DG_DEFINE_CONFIG(FN, BN_, ST_, AC_, MH_) DG_DEFINE_CONFIG_KS(FN, BN_, ST_, AC_, MH_, 1)
 // With the epilogue variants.

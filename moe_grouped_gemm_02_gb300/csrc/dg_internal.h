@@ -84,6 +84,7 @@ struct KernelConfig {
     GemmLaunchFn launch_act;   // with bias, activation and residual in the epilogue; null: not instantiated
     size_t (*act_smem)(int split);   // shared memory that launch_act takes on top of smem_bytes
     cudaError_t (*prepare)(int max_smem);   // per-device one-time kernel attribute setup
+    cudaError_t (*prepare_act)(int max_smem);   // the same for launch_act's kernels
     int (*max_clusters)(int split, size_t smem);   // co-resident clusters of `split` CTAs
 };
 

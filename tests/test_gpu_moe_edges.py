@@ -184,3 +184,47 @@ def test_tensors_of_another_device_are_refused():
         dg.dg_moe_sort_masked(here, far, n, 8)
     with pytest.raises(ValueError, match="current CUDA device"):
         dg.dg_moe_route(far_logits, far, far_w)
+
+
+# ---------------------------------------------------------------------------------------------
+# First calls of a process
+# ---------------------------------------------------------------------------------------------
+FIRST_CALLS = """
+import os
+import torch
+import moe_grouped_gemm_02_gb300 as dg
+M, N, K = 256, 512, 512
+a, b = (torch.randint(0, 0x70, (r, K), dtype=torch.uint8, device="cuda") for r in (M, N))
+sfa, sfb = (torch.full(dg.packed_sf_shape(None, r, K), 0x77777777, dtype=torch.int32, device="cuda") for r in (M, N))
+d, d1, d2 = (torch.zeros((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+torch.cuda.synchronize()
+free = torch.cuda.mem_get_info()[0]
+dg.dg_fp8_gemm_nt(a, sfa, b, sfb, d)
+torch.cuda.synchronize()
+print("plain", free - torch.cuda.mem_get_info()[0])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dg.dg_fp8_gemm_nt_act(a, sfa, b, sfb, d1, act="gelu")
+    os.environ["DG_FORCE_CONFIG"] = "config_bn32_s8_a2"
+    dg.dg_fp8_gemm_nt_act(a, sfa, b, sfb, d2, act="gelu")
+    del os.environ["DG_FORCE_CONFIG"]
+g.replay()
+dg.dg_fp8_gemm_nt_act(a, sfa, b, sfb, d, act="gelu")
+dg.dg_check_device_error()
+assert torch.equal(d, d1) and torch.allclose(d.float(), d2.float(), rtol=2.0 ** -7)
+print("captured")
+"""
+
+
+def test_plain_gemm_loads_no_epilogue_kernels():
+    # a process that only multiplies holds the plain kernels, 4 MB of the device's memory; with the epilogues' it was
+    # 16 MB.  And the epilogues' first call may be under capture
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    out = r.stdout.split()
+    assert out[0] == "plain" and out[2] == "captured"
+    assert int(out[1]) <= 8 << 20
