@@ -295,7 +295,8 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_act(const void* a, const int32_t* sfa,
  *   dd         BF16 [rows][N] ([rows][N / 2] with DG_ACT_SWIGLU): gradient of D
  *   z          BF16 [rows][N]: the kept pre-activations
  *   m_indices  int32 [rows] as for the contiguous layout (rows % 128 == 0), or NULL (dense, G = 1)
- *   dz         BF16 [rows][N]: gradient of A @ B^T + bias; rows with m_indices -1 are zeros
+ *   dz         BF16 [rows][N]: gradient of A @ B^T + bias; rows with m_indices -1 (with dbias: outside
+ *              [0, G), as the GEMM takes them) are zeros
  *   dbias      FP32 [G][N]: column sums, over each expert's rows, of the unrounded dz; or NULL
  *   workspace  FP32 [ceil(rows / 128)][N], needed with dbias
  * Requires N % 8 == 0 (DG_ACT_SWIGLU: 16), G <= 4096.  The sums have a fixed order.

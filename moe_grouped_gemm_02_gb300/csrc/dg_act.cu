@@ -14,6 +14,7 @@
 #include "dg_ptx.cuh"
 
 #include <algorithm>
+#include <climits>
 
 namespace dg {
 
@@ -36,7 +37,7 @@ template <int ACT>
 __global__ void __launch_bounds__(32 * AB_WARPS)
     act_backward_kernel(const uint16_t* __restrict__ dd, const uint16_t* __restrict__ z,
                         const int32_t* __restrict__ m_indices, uint16_t* __restrict__ dz, float* __restrict__ part,
-                        int rows, int N, int strips) {
+                        int rows, int N, int experts, int strips) {
     constexpr bool GATED = ACT == ACT_SWIGLU;
     __shared__ float sums[AB_WARPS][AB_COLS];
     griddep_wait();
@@ -57,7 +58,9 @@ __global__ void __launch_bounds__(32 * AB_WARPS)
         for (int u = 0; u < 4; ++u) {
             const long long row = 128LL * block + AB_ROWS * warp + r0 + u;
             live[u] = in && row < rows;
-            valid[u] = live[u] && (m_indices == nullptr || __ldg(m_indices + row) >= 0);
+            // (-1 is past every expert as an unsigned number)
+            valid[u] = live[u] && (m_indices == nullptr ||
+                                   static_cast<uint32_t>(__ldg(m_indices + row)) < static_cast<uint32_t>(experts));
             zv[u] = make_uint4(0u, 0u, 0u, 0u);
             dv[u] = zv[u];
             if (valid[u]) {
@@ -182,6 +185,7 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long long
 cudaError_t launch_act_backward(const void* dd, const void* z, const int32_t* m_indices, void* dz, float* dbias,
                                 float* part, int rows, int N, int G, int act, int pdl, cudaStream_t stream) {
     const int blocks = (rows + 127) / 128, strips = (N + AB_COLS - 1) / AB_COLS;
+    const int experts = dbias ? G : INT_MAX;      // (without dbias nothing says how many there are)
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     cudaError_t e;
@@ -190,7 +194,7 @@ cudaError_t launch_act_backward(const void* dd, const void* z, const int32_t* m_
         if (e != cudaSuccess) return e;
         auto go = [&](auto kernel) {
             return cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint16_t*>(dd), static_cast<const uint16_t*>(z),
-                                      m_indices, static_cast<uint16_t*>(dz), dbias ? part : nullptr, rows, N, strips);
+                                      m_indices, static_cast<uint16_t*>(dz), dbias ? part : nullptr, rows, N, experts, strips);
         };
         e = act == ACT_RELU     ? go(act_backward_kernel<ACT_RELU>)
             : act == ACT_GELU   ? go(act_backward_kernel<ACT_GELU>)

@@ -228,3 +228,28 @@ def test_plain_gemm_loads_no_epilogue_kernels():
     out = r.stdout.split()
     assert out[0] == "plain" and out[2] == "captured"
     assert int(out[1]) <= 8 << 20
+
+
+# ---------------------------------------------------------------------------------------------
+# Activation gradient: rows of no expert
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("act", ACTS)
+def test_rows_past_the_last_expert_have_no_gradient(act):
+    # the GEMM writes zeros to rows whose expert index is outside [0, G), and the bias gradient leaves them out:
+    # their dz is zeros too, and neither their z nor their dd is read
+    N, G, H = 272, 2, 136 if act == "swiglu" else 272
+    m = torch.tensor([0] * 100 + [-1] * 28 + [1] * 128 + [2] * 128 + [4096] * 128, dtype=torch.int32, device="cuda")
+    rows = m.numel()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = torch.randn((rows, N), generator=g, device="cuda").to(torch.bfloat16)
+    dd = torch.randn((rows, H), generator=g, device="cuda").to(torch.bfloat16)
+    inside = (m >= 0) & (m < G)
+    z[~inside], dd[~inside] = float("nan"), float("nan")
+    dz, db = torch.full_like(z, 7.0), torch.full((G, N), 7.0, device="cuda")
+    ws = _empty(*dg.act_backward_workspace_shape(rows, N), dtype=torch.float32)
+    dg.dg_act_backward(dd, z, dz, act=act, dbias=db, workspace=ws, m_indices=m)
+    assert torch.all(dz[~inside] == 0)
+    # the inside: bit for bit what the same rows give under -1 padding
+    dz2, db2 = torch.empty_like(z), torch.empty_like(db)
+    dg.dg_act_backward(dd, z, dz2, act=act, dbias=db2, workspace=ws, m_indices=torch.where(inside, m, -1))
+    assert torch.equal(dz[inside], dz2[inside]) and torch.equal(db, db2) and bool(dz[inside].isfinite().all())
