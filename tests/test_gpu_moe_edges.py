@@ -253,3 +253,116 @@ def test_rows_past_the_last_expert_have_no_gradient(act):
     dz2, db2 = torch.empty_like(z), torch.empty_like(db)
     dg.dg_act_backward(dd, z, dz2, act=act, dbias=db2, workspace=ws, m_indices=torch.where(inside, m, -1))
     assert torch.equal(dz[inside], dz2[inside]) and torch.equal(db, db2) and bool(dz[inside].isfinite().all())
+
+
+# ---------------------------------------------------------------------------------------------
+# Epilogues: the residual in place, values that are not finite
+# ---------------------------------------------------------------------------------------------
+def _operands(lead_a, lead_b, rows, N, K, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    # codes of +-[2^-3, 7.5]: finite, so sums of any order differ in rounding only; scales 2^-4 .. 2^-1
+    a, b = (torch.randint(0x20, 0x50, (*s, K), generator=g, device="cuda").to(torch.uint8) |
+            (torch.randint(0, 2, (*s, K), generator=g, device="cuda") << 7).to(torch.uint8) for s in ((*lead_a, rows), (*lead_b, N)))
+    def scales(lead, r):
+        kp, al = dg.packed_sf_shape(None, r, K)
+        by = torch.randint(123, 127, (*lead, kp, al, 4), generator=g, device="cuda")
+        return (by << torch.tensor([0, 8, 16, 24], device="cuda")).sum(-1).to(torch.int32)
+    return a, scales(lead_a, rows), b, scales(lead_b, N)
+
+
+def _case(layout, rows, G, N, K, act, seed=1):
+    """call(d, **extras) of one layout, D's shape and z's."""
+    lead = (G,) if layout == "masked" else ()
+    a, sfa, b, sfb = _operands(lead, () if layout == "dense" else (G,), rows, N, K, seed)
+    H = N // 2 if act == "swiglu" else N
+    if layout == "dense":
+        return (lambda d, **x: dg.dg_fp8_gemm_nt_act(a, sfa, b, sfb, d, act=act, **x)), (rows, H), (N,)
+    if layout == "contiguous":
+        # expert e: 128 rows for every second block, the last of them padded
+        m = torch.arange(rows, device="cuda").div(256, rounding_mode="floor").clamp(max=G - 1).to(torch.int32)
+        m[rows - 37:] = -1
+        return (lambda d, **x: dg.dg_m_grouped_fp8_gemm_nt_contiguous_act(a, sfa, b, sfb, d, m, act=act, **x)), (rows, H), (G, N)
+    m = torch.tensor([rows, 1, 0, rows - 3][:G], dtype=torch.int32, device="cuda")
+    return (lambda d, **x: dg.dg_m_grouped_fp8_gemm_nt_masked_act(a, sfa, b, sfb, d, m, act=act, **x)), (G, rows, H), (G, N)
+
+
+# layout, rows, G, N, K, configuration, split, SMs (0: all): every way the epilogues read the residual, with one tile per CTA and with several
+PLANS = [("dense", 300, 1, 720, 384, c, 1, s) for c in ("config_bn224_s3_m2", "config_bn192_s3_m2", "config_bn192_s5_k2", "config_bn128_s5_k2",
+                                                        "config_bn224_s4_a2", "config_bn64_s8_a2", "config_bn32_s8_a2") for s in (0, 4)] + \
+        [("dense", 61, 1, 720, 384, "config_bn128_s8_k2_r64", 1, s) for s in (0, 4)] + \
+        [("dense", 130, 1, 464, 2048, c, p, s) for c in ("config_bn128_s5_k2", "config_bn64_s8_a2", "config_bn32_s8_a2")
+         for p, s in ((2, 0), (4, 16), (8, 0))] + \
+        [("dense", 50, 1, 464, 2048, "config_bn128_s8_k2_r64", p, s) for p, s in ((2, 16), (8, 0))] + \
+        [("contiguous", 896, 4, 464, 640, c, 1, s) for c in ("config_bn224_s3_m2", "config_bn192_s3_m2", "config_bn128_s5_k2", "config_bn224_s4_a2")
+         for s in (0, 4)] + \
+        [("masked", 200, 4, 320, 1024, c, p, s) for c, p, s in (("config_bn128_s5_k2", 1, 0), ("config_bn128_s5_k2", 4, 0),
+                                                                 ("config_bn224_s4_a2", 1, 4), ("config_bn64_s8_a2", 2, 16))] + \
+        [("masked", 600, 2, 320, 512, "config_bn224_s3_m2", 1, s) for s in (0, 4)]
+
+
+def _planned(monkeypatch, cfg, split, sms):
+    monkeypatch.setenv("DG_FORCE_CONFIG", cfg)
+    monkeypatch.setenv("DG_FORCE_SPLIT", str(split))
+    dg.dg_set_num_sms(sms)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("layout,rows,G,N,K,cfg,split,sms", PLANS)
+def test_residual_in_place(act, layout, rows, G, N, K, cfg, split, sms, monkeypatch):
+    # D as its own residual: the bits of the call with a residual of its own
+    call, shape, bias_shape = _case(layout, rows, G, N, K, act)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    res = (3 * torch.randn(shape, generator=g, device="cuda")).to(torch.bfloat16)
+    bias = torch.randn(bias_shape, generator=g, device="cuda")
+    apart, inplace = res.clone(), res.clone()           # (rows that the call leaves alone are the same in both)
+    _planned(monkeypatch, cfg, split, sms)
+    try:
+        call(apart, bias=bias, residual=res)
+        call(inplace, bias=bias, residual=inplace)
+    finally:
+        dg.dg_set_num_sms(0)
+    dg.dg_check_device_error()
+    assert torch.equal(apart.view(torch.int16), inplace.view(torch.int16))
+    assert not torch.equal(apart, res)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("layout,rows,G,N,K,cfg,split,sms", PLANS)
+def test_values_that_are_not_finite_stay_in_their_place(act, layout, rows, G, N, K, cfg, split, sms, monkeypatch):
+    # a bias of infinities and NaN in one column of some pairs (the first or the second): the other columns
+    # hold the same values as without, and the column itself the activation's limit.  SiLU and GELU divide by the
+    # product of a pair's denominators, so the column beside it may round to the next BF16 value; all others hold
+    # the same bits
+    call, shape, bias_shape = _case(layout, rows, G, N, K, act)
+    bias = torch.randn(bias_shape, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    odd = bias.clone()
+    cols = torch.arange(0, N, 6, device="cuda") + (torch.arange(0, N, 6, device="cuda") // 6) % 2
+    cols = cols[cols < N]
+    kinds = torch.arange(cols.numel(), device="cuda") // 2 % 3
+    values = torch.tensor([float("inf"), float("-inf"), float("nan")], device="cuda")
+    odd[..., cols] = values[kinds]
+    d0, d1 = torch.zeros(shape, dtype=torch.bfloat16, device="cuda"), torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    _planned(monkeypatch, cfg, split, sms)
+    try:
+        call(d0, bias=bias)
+        call(d1, bias=odd)
+    finally:
+        dg.dg_set_num_sms(0)
+    dg.dg_check_device_error()
+    at = cols // 2 if act == "swiglu" else cols
+    clean = torch.ones((shape[-1],), dtype=torch.bool, device="cuda")
+    clean[at] = False
+    apart = (d0[..., clean].view(torch.int16).int() - d1[..., clean].view(torch.int16).int()).abs()
+    assert int(apart.max()) <= (1 if act in ("silu", "gelu") else 0)
+    beside = torch.zeros_like(clean)
+    beside[at ^ 1] = True
+    assert int(apart[..., ~beside[clean]].max()) == 0
+    assert bool(d0.isfinite().all())
+    if act == "swiglu":
+        return
+    live = d0.abs().sum(-1) > 0                         # rows that the call computes
+    got = d1[live][:, cols].float()
+    assert bool(live.any())
+    low = {"none": float("-inf"), "relu": 0.0}.get(act)
+    assert bool((got[:, kinds == 0] == float("inf")).all()) and bool(got[:, kinds == 2].isnan().all())
+    assert bool((got[:, kinds == 1] == low).all() if low is not None else (got[:, kinds == 1].abs() <= 1e-17).all())
