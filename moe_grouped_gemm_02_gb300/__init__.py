@@ -318,7 +318,9 @@ def _addr(stream):
 
 
 def dg_moe_max_rows(T: int, k: int, G: int) -> int:
-    """Rows the contiguous layout of T tokens with k choices among G experts can need."""
+    """Rows the contiguous layout of T tokens with k choices among G experts can need, -1 past 2^31 - 1."""
+    if max(T, k, G) >= 1 << 31 or min(T, k, G) < 0:      # (past the C call's int, which would wrap)
+        return -1
     return load_library().dg_moe_max_rows(int(T), int(k), int(G))
 
 

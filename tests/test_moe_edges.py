@@ -97,3 +97,11 @@ def test_launchers_keep_no_state_between_calls():
         text = open(os.path.join(dg_build.CSRC, name)).read()
         found = re.findall(r"^(?:static |inline |__device__ )*[\w:]+ \**g_\w+ *(?:=|;|\[).*$", text, re.M)
         assert found == [], name
+
+
+def test_max_rows_of_sizes_past_an_int(lib):
+    big = 1 << 32
+    for T, k, G in ((big + 5, 1, 4), (5, big + 1, 4), (5, 1, big + 4), (1 << 31, 1, 4), (7 - big, 1, 4), (5, -1, 4)):
+        assert dg.dg_moe_max_rows(T, k, G) == -1
+    assert dg.dg_moe_max_rows(5, 2, 4) == 512
+    assert dg.dg_moe_max_rows((1 << 31) - 1, 1, 1) == -1 and dg.dg_moe_max_rows((1 << 31) - 256, 1, 1) == (1 << 31) - 256
