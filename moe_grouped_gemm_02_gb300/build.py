@@ -48,6 +48,11 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(p) > t for p in [src] + _headers())
 
 
+def _older(out: str, parts) -> bool:
+    """Whether `out` is missing or was linked before one of its parts was compiled."""
+    return not os.path.exists(out) or any(os.path.getmtime(p) > os.path.getmtime(out) for p in parts)
+
+
 def _run(cmd, what: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -89,7 +94,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, r.returncode, r.stdout + r.stderr
 
-    binding = force or _stale(BINDING_OBJ, BINDING_SRC) or not os.path.exists(BINDING_PATH)
+    binding = force or _stale(BINDING_OBJ, BINDING_SRC)
     if todo or binding:
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(todo) + 1, os.cpu_count() or 4)) as ex:
             done = ex.submit(_compile_binding) if binding else None
@@ -100,7 +105,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
                     raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
             if done is not None:
                 done.result()
-    if todo or not os.path.exists(LIB_PATH):
+    # (by the files, not by what was compiled just now: a build that failed halfway left parts behind)
+    if _older(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp"
         # (the soname is what dg_binding.so records: it finds the library in its own folder)
         cmd = [nvcc, *GENCODE, "-shared", "-Xlinker", "-soname=libdg.so", "-o", tmp, *objs]
@@ -109,7 +115,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libdg.so failed")
         os.replace(tmp, LIB_PATH)
-    if binding:
+    if _older(BINDING_PATH, [BINDING_OBJ]):
         _link_binding()
     return LIB_PATH
 

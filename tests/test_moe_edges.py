@@ -105,3 +105,54 @@ def test_max_rows_of_sizes_past_an_int(lib):
         assert dg.dg_moe_max_rows(T, k, G) == -1
     assert dg.dg_moe_max_rows(5, 2, 4) == 512
     assert dg.dg_moe_max_rows((1 << 31) - 1, 1, 1) == -1 and dg.dg_moe_max_rows((1 << 31) - 256, 1, 1) == (1 << 31) - 256
+
+
+def test_a_build_that_failed_halfway_is_completed(tmp_path, monkeypatch):
+    # the binding compiles, a kernel file does not: the next build links both anew.  (nvcc and g++ are stand-ins
+    # that write their output files)
+    src, out = tmp_path / "csrc", tmp_path / "out"
+    src.mkdir(), out.mkdir()
+    for name in ("one.cu", "two.cu", "dg_binding.cpp"):
+        (src / name).write_text("first")
+    nvcc = tmp_path / "nvcc"
+    nvcc.write_text("""#!/bin/sh
+log="$LOG"; prev=""; out=""
+for a in "$@"; do
+    [ "$prev" = "-o" ] && out="$a"
+    case "$a" in *.cu) grep -q broken "$a" && exit 1;; esac
+    prev="$a"
+done
+echo "$out" >> "$log"; touch "$out"
+""")
+    nvcc.chmod(0o755)
+    log = tmp_path / "log"
+    for k, v in {"CSRC": src, "INCLUDE": src, "BUILD_DIR": out, "LIB_PATH": out / "libdg.so", "BINDING_SRC": src / "dg_binding.cpp",
+                 "BINDING_OBJ": out / "dg_binding.o", "BINDING_PATH": out / "dg_binding.so"}.items():
+        monkeypatch.setattr(dg_build, k, str(v))
+    monkeypatch.setenv("NVCC", str(nvcc))
+    monkeypatch.setenv("LOG", str(log))
+
+    def run(cmd, what):
+        target = cmd[cmd.index("-o") + 1]
+        with open(log, "a") as f:
+            f.write(target + "\n")
+        open(target, "w").close()
+    monkeypatch.setattr(dg_build, "_run", run)
+
+    def built():
+        log.write_text("")
+        dg_build.build()
+        return {os.path.basename(x) for x in log.read_text().split()}
+
+    assert built() == {"one.o", "two.o", "dg_binding.o", "libdg.so.tmp", "dg_binding.so.tmp"}
+    assert built() == set()
+    past = os.stat(out / "dg_binding.so").st_mtime - 100         # everything so far is old; then two files change
+    for p in list(src.iterdir()) + list(out.iterdir()):
+        os.utime(p, (past, past))
+    (src / "dg_binding.cpp").write_text("second")
+    (src / "two.cu").write_text("broken")
+    with pytest.raises(RuntimeError):
+        built()
+    (src / "two.cu").write_text("second")
+    assert built() == {"two.o", "libdg.so.tmp", "dg_binding.so.tmp"}
+    assert built() == set()
