@@ -341,7 +341,8 @@ int dg_moe_max_rows(int T, int k, int G);
  *              group sizes of dg_k_grouped_fp8_gemm_tn_contiguous), or NULL
  *   slots whose row would be at or past `rows` have none
  * dg_moe_sort_masked, masked layout: slot number m of expert g has row g * max_m + m; slots at or
- *   past max_m have none;  masked_m  int32 [G]: min(count, max_m)
+ *   past max_m have none (max_m >= 1, or 0 without tokens);  masked_m  int32 [G]: min(count, max_m)
+ * pos does not overlap topk_idx.
  * Requires k <= 32, G <= 4096.  One launch, nothing read back: capturable in a CUDA graph.
  */
 dg_status dg_moe_sort(const int32_t* topk_idx, int32_t* pos, int32_t* m_indices, int32_t* counts, int32_t* ks, int T,

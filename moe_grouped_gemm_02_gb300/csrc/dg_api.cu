@@ -881,9 +881,9 @@ dg_status dg_moe_sort(const int32_t* topk_idx, int32_t* pos, int32_t* m_indices,
 
 dg_status dg_moe_sort_masked(const int32_t* topk_idx, int32_t* pos, int32_t* masked_m, int T, int k, int G, int max_m,
                              void* stream) {
-    if ((T != 0 && (!topk_idx || !pos)) || !masked_m || max_m <= 0) return DG_ERR_INVALID_ARG;
+    if ((T != 0 && (!topk_idx || !pos)) || !masked_m || max_m < 0 || (T != 0 && max_m == 0)) return DG_ERR_INVALID_ARG;
     if (static_cast<long long>(G) * max_m > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
-    return run_sort(topk_idx, pos, nullptr, masked_m, nullptr, T, k, G, 0, max_m, stream);
+    return run_sort(topk_idx, pos, nullptr, masked_m, nullptr, T, k, G, 0, std::max(max_m, 1), stream);
 }
 
 dg_status dg_moe_dispatch_fp8(const void* x, const int32_t* pos, const int32_t* m_indices, void* q, int32_t* sf, int T,

@@ -47,6 +47,23 @@ def test_epilogues_without_rows(act):
     assert torch.all(db == 0)
 
 
+def test_masked_layout_without_tokens():
+    # a decode step of no tokens: a layout of no rows per group
+    G, K, k = 5, 256, 2
+    i32 = torch.int32
+    idx, pos, w, n = _empty(0, k, dtype=i32), _empty(0, k, dtype=i32), _empty(0, k, dtype=torch.float32), torch.full((G,), 7, dtype=i32, device="cuda")
+    dg.dg_moe_route(_empty(0, G, dtype=torch.float32), idx, w)
+    dg.dg_moe_sort_masked(idx, pos, n, 0)
+    assert n.tolist() == [0] * G
+    x, y = _empty(0, K), _empty(0, K)
+    dg.dg_moe_dispatch_fp8(x, pos, _empty(G, 0, K, dtype=torch.uint8), _empty(*dg.packed_sf_shape(G, 0, K), dtype=i32))
+    dg.dg_moe_combine(_empty(G, 0, K), pos, w, y, residual=x)
+    with pytest.raises(dg.DGError):
+        dg.dg_moe_sort_masked(torch.zeros((1, k), dtype=i32, device="cuda"), _empty(1, k, dtype=i32), n, 0)
+    with pytest.raises(dg.DGError):
+        dg.dg_moe_sort_masked(idx, pos, n, -1)
+
+
 def test_layer_without_tokens():
     # forward and backward of the example layer on a rank without tokens: every weight's gradient is zeros
     import importlib.util
