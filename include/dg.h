@@ -273,8 +273,9 @@ enum { DG_ACT_NONE = 0, DG_ACT_RELU = 1, DG_ACT_GELU = 2, DG_ACT_SILU = 3, DG_AC
  *             DG_ACT_SWIGLU  column pairs (2j, 2j+1) of A @ B^T are (gate, up):
  *                            h_j = gate sigmoid(gate) up; the rows of B interleave the gate and
  *                            the up projection; N % 16 == 0
- * act(v) takes the unrounded v; D is rounded once.  Contiguous: rows with m_indices -1 are +0.0 in
- * D and z.  Masked: rows at or past masked_m[g] of D and z are left untouched.
+ * act(v) takes the unrounded v; D is rounded once.  Where SiLU or GELU is below 1e-17 in size (v below
+ * about -43 and -7.5), act(v) is within 1e-17 of it and may be larger in size.  Contiguous: rows with
+ * m_indices -1 are +0.0 in D and z.  Masked: rows at or past masked_m[g] of D and z are left untouched.
  */
 dg_status dg_fp8_gemm_nt_act(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb, const void* bias,
                              const void* residual, void* z, void* d, int M, int N, int K, int act, int bias_dtype,
@@ -299,7 +300,8 @@ dg_status dg_m_grouped_fp8_gemm_nt_masked_act(const void* a, const int32_t* sfa,
  *              [0, G), as the GEMM takes them) are zeros
  *   dbias      FP32 [G][N]: column sums, over each expert's rows, of the unrounded dz; or NULL
  *   workspace  FP32 [ceil(rows / 128)][N], needed with dbias
- * Requires N % 8 == 0 (DG_ACT_SWIGLU: 16), G <= 4096.  The sums have a fixed order.
+ * Requires N % 8 == 0 (DG_ACT_SWIGLU: 16), G <= 4096.  The sums have a fixed order, in FP32, of terms good
+ * to a few FP32 units of |dd| max(1, |z|).
  */
 dg_status dg_act_backward(const void* dd, const void* z, const int32_t* m_indices, void* dz, float* dbias,
                           float* workspace, int rows, int N, int G, int act, void* stream);

@@ -17,8 +17,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // 1 / (1 + e^-x).  The approximate 2^x and reciprocal are good to a few FP32 rounding steps (the
-// product with log2 e adds ~1e-6 at |x| = 20), far below the BF16 rounding of what is computed from it;
-// a large -x gives 0, a large x 1.
+// product with log2 e adds ~1e-6 at |x| = 20, where the result or its distance from 1 is below 2e-9), far below the
+// BF16 rounding of D, z and dz; a large -x gives 0, a large x 1.  The FP32 bias gradient sums slopes computed
+// from it: over all BF16 z up to 60 they are off by at most 2^-23.1 (silu), 2^-21.3 (gelu), 2^-23.0 (swiglu) of
+// max(1, |z|), as much as with expf and a division in FP32 (2^-23.1, 2^-21.3, 2^-23.0).
 constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float act_sigmoid(float x) { return rcp_approx(1.0f + ex2_approx(-LOG2E * x)); }
 
@@ -46,7 +48,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // e = 2^(-a log2 e), 1/(1 + e0) = (1 + e1) / ((1 + e0)(1 + e1)), so a value costs one and a half
 // operations of the special function unit, which bounds the epilogue of a tile with a short K, instead of
 // two.  e is held at 2^62, so that the product stays finite, and v at -43 in the result: below a = -43, where
-// |act| < 1e-17, the result is -1e-17 at most instead of smaller still.
+// |act| < 1e-17, the result is -1e-17 at most instead of smaller still.  (A value's last FP32 bits depend on the other
+// one's through the shared rounding: D may be the next BF16 value.)
 template <int ACT>
 __device__ __forceinline__ void act_two(float v0, float v1, float& h0, float& h1) {
     if constexpr (ACT == ACT_SILU || ACT == ACT_GELU) {

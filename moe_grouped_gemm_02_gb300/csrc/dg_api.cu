@@ -466,8 +466,8 @@ dg_status run_gemm(const GemmCall& call, void* stream) {
     args.residual = static_cast<const uint16_t*>(call.residual);
     args.z = static_cast<uint16_t*>(call.z);
     // A residual that is likely still in L2 gains nothing from a prefetch and pays its instructions: 256-row
-    // tiles, GELU + residual, with / without: 11595 x 2048 x 1536 (47 MB) 52.5 / 50.0 us, 10782 x 3696 x 640 (80 MB)
-    // 84 / 93 us, 12995 x 4240 x 2560 (110 MB) 130 / 135 us.
+    // tiles, GELU + residual, with / without: 11595 x 2048 x 1536 (47 MB) 51.2 / 49.3 us, 10782 x 3696 x 640 (80 MB)
+    // 64 / 76 us, 12995 x 4240 x 2560 (110 MB) 138 / 143 us.
     args.prefetch_residual =
         call.residual && static_cast<double>(rows) * DN * 2.0 * (mode == MODE_MASKED ? groups : 1) > 64.0 * 1024 * 1024;
     args.err = st->err_ptr;

@@ -498,7 +498,7 @@ __device__ __forceinline__ void acc_ld(uint32_t taddr, uint32_t (&r)[32]) {
 // Against the GEMM without an epilogue (us, back to back): 32768 tokens of 4 experts, 4096 x 7168, SwiGLU
 // and bias 650 / 645, with z 700 (both at the power cap; z is 271 MB more to write); 4 x 256 masked rows, 7168 x
 // 2048, SwiGLU 17.0 / 17.1; 64 x 2112 x 7168, GELU, bias and residual 7.9 / 7.5; with a short K the
-// epilogue's arithmetic shows: 10782 x 3696 x 640, SiLU and bias 61 / 43.
+// epilogue's arithmetic shows: 10782 x 3696 x 640, SiLU and bias 46 / 33.
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& w, float (&f)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};

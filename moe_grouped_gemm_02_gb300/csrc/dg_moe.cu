@@ -58,8 +58,9 @@ cudaError_t launch_cfg(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long 
 // bits: ties go to the lowest lane, and the chosen keys' indices are found afterwards, all k at
 // once, by searching the row segment of the lane that gave each.
 //
-// Bound by instruction issue: ~240 per token at 256 experts and k = 8 (32768 tokens: 10.2 us, 1.8 of it the launch;
-// its 19 MB cross HBM in 2.8).
+// 32768 tokens, 256 BF16 experts, k = 8: 10.2 us; its 19 MB cross HBM in 2.8.  Bound by instructions and by the
+// latencies between them: 241 instructions per token take the schedulers 6.8 us of it (59 % of the active cycles), the
+// launch 1.8; in between the warps wait for a token's loads, the ALU pipe and the redux of one choice before the next.
 constexpr int ROUTE_WARPS = 4;
 constexpr int ROUTE_CTAS = 152 * 16;     // CTAs that get one token per warp; with more, warps take several
 
@@ -198,7 +199,7 @@ __device__ __forceinline__ float sigmoid_over(float x, float top) {
 
 // group: tokens whose choices share the lanes of the last steps (scores, sums, stores), each
 // with slot lanes (a power of two >= k).
-// (12 CTAs per SM leave 40 registers: at the compiler's own choice of 31, 32768 x 256 BF16 took 11.1 us, now 10.2.)
+// (12 CTAs per SM leave 40 registers: at the compiler's own choice of 31, 32768 x 256 BF16 took 11.1 us instead of 10.2.)
 template <int NV, bool F32>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV <= 8 ? 12 : 0)
     route_kernel(const void* __restrict__ logits, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, int T,
@@ -832,7 +833,8 @@ constexpr int COMBINE_WARPS = 8;
 constexpr int COMBINE_FEW = 152 * 32;    // warps that hold 64 registers each on all SMs at once
 
 // One warp per token and U x 512 bytes of the row; the k rows' units are summed in j order in FP32 (an output
-// element belongs to one thread: no atomics, no order to vary).  ROWS x U units are in flight per lane.
+// element belongs to one thread: no atomics, no order to vary).  Up to ROWS x U units are in flight per lane (the
+// FP32 kernel for eight rows compiles to 34 registers, so that some of its loads wait for others' values).
 // Bound by HBM: 16384 tokens x 8, N 7168 BF16, 2.1 GB in 303 us, 6.9 TB/s.
 template <bool F32, int ROWS, int U>
 __global__ void __launch_bounds__(32 * COMBINE_WARPS)
@@ -1108,7 +1110,8 @@ cudaError_t launch_moe_dispatch_fp8(const void* x, const int32_t* pos, const int
     const int pad_chunks = padding_chunks(rows, K / 16);
     // Two spans per warp, and so twice the loads in flight, where few stores follow each load or the spans fill the GPU
     // many times over (us, two / one: 16384 tokens x 1, K 7168 62 / 85; 16384 x 2, K 4096 46 / 57; 16384 x 8,
-    // K 7168 190 / 192; 4000 x 8, K 7168 57 / 54; 64 x 8, K 7168 5.1 / 4.5).
+    // K 7168 190 / 192; 4000 x 3, K 7168 28.7 / 31.3, x 4 30.4 / 31.0, x 5 37.5 / 37.5, x 8 57 / 54; 64 x 8, K 7168
+    // 5.1 / 4.5).
     const long long spans = static_cast<long long>(T) * Kp;
     const int U = Kp > 1 && (spans > 65536 || (k <= 4 && spans > 152 * 64)) ? DISPATCH_U : 1;
     const long long units = static_cast<long long>(T) * ((Kp + U - 1) / U) + (m_indices ? static_cast<long long>(rows / PAD_ROWS) * pad_chunks : 0);
