@@ -23,8 +23,9 @@
  *  - Every pointer is a DEVICE pointer owned by the caller.  The library allocates and frees
  *    no memory in any of these calls.
  *  - All tensors are dense and row-major (last dimension contiguous) with the shapes given.
- *  - Every pointer must be 16-byte aligned (TMA requirement), else DG_ERR_ALIGNMENT.  A pointer to
- *    a tensor without elements (no tokens, no rows) may be NULL.
+ *  - Every pointer must be 16-byte aligned (TMA requirement), else DG_ERR_ALIGNMENT.  (Indices,
+ *    counts and weights that are read word by word pass with 4 bytes.)  A pointer to a tensor without
+ *    elements (no tokens, no rows) may be NULL.
  *  - Calls are asynchronous on `stream` (a cudaStream_t passed as void*; NULL means the
  *    legacy default stream).  They never synchronize, except in validation mode (the
  *    environment variable DG_VALIDATE=1), where the device-side contracts below are read

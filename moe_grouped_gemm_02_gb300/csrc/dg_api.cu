@@ -144,6 +144,13 @@ int effective_sms(const DeviceState& st) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Indices, counts and weights, which the kernels read word by word: slices of a tensor may pass, words across a word
+// boundary, which the GPU cannot read, may not.
+template <class... P>
+bool aligned4(const P*... p) {
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
+
 int al4(int x) { return (x + 3) / 4 * 4; }
 
 // 3-D tiled map; row_bytes is the pitch of dimension 1 (d0 elements, which for packed 4-bit
@@ -316,6 +323,7 @@ dg_status run_gemm(const GemmCall& call, void* stream) {
     const int32_t* m_indices = call.m_indices;
     const int32_t* masked_m = call.masked_m;
     const int groups = call.groups, b_groups = call.b_groups, rows = call.rows, N = call.N, K = call.K;
+    if (!aligned4(m_indices, masked_m, call.ks)) return DG_ERR_ALIGNMENT;
     DeviceState* st = nullptr;
     dg_status s = current_device(&st);
     if (s != DG_OK) return s;
@@ -589,6 +597,7 @@ dg_status run_sort(const int32_t* topk_idx, int32_t* pos, int32_t* m_indices, in
     if (T < 0 || k <= 0 || G <= 0) return DG_ERR_INVALID_ARG;
     if (k > kMaxChoices || G > kMaxMaskedGroups || static_cast<long long>(T) * k > 0x7FFFFFFFLL - 1024 - 128LL * G)
         return DG_ERR_SHAPE;
+    if (!aligned4(topk_idx, pos, counts, ks)) return DG_ERR_ALIGNMENT;
     DeviceState* st = nullptr;
     const dg_status s = current_device(&st);
     if (s != DG_OK) return s;
@@ -891,7 +900,7 @@ dg_status dg_moe_dispatch_fp8(const void* x, const int32_t* pos, const int32_t* 
     if ((T != 0 && (!x || !pos)) || (rows != 0 && (!q || !sf)) || T < 0 || k <= 0 || K <= 0 || G <= 0 || rows < 0) return DG_ERR_INVALID_ARG;
     if (k > kMaxChoices || K % 128 != 0 || static_cast<long long>(G) * rows > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
     if (m_indices && (G != 1 || rows % 128 != 0)) return DG_ERR_SHAPE;
-    if (!aligned16(x) || !aligned16(m_indices) || !aligned16(q) || !aligned16(sf)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(x) || !aligned4(pos) || !aligned16(m_indices) || !aligned16(q) || !aligned16(sf)) return DG_ERR_ALIGNMENT;
     if (T == 0 || rows == 0) return DG_OK;
     DeviceState* st = nullptr;
     const dg_status s = current_device(&st);
@@ -908,7 +917,7 @@ dg_status dg_moe_dispatch(const void* x, const int32_t* pos, const int32_t* m_in
     int n16 = 0;
     dg_status s = check_rows(T, k, K, rows, dtype, m_indices, &n16);
     if (s != DG_OK) return s;
-    if (!aligned16(x) || !aligned16(m_indices) || !aligned16(out)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(x) || !aligned4(pos) || !aligned16(m_indices) || !aligned16(out)) return DG_ERR_ALIGNMENT;
     if (T == 0 || rows == 0) return DG_OK;
     DeviceState* st = nullptr;
     if ((s = current_device(&st)) != DG_OK) return s;
@@ -924,7 +933,7 @@ dg_status dg_moe_combine(const void* yp, const int32_t* pos, const float* w, con
     int n16 = 0;
     dg_status s = check_rows(T, k, N, rows, dtype, nullptr, &n16);
     if (s != DG_OK) return s;
-    if (!aligned16(yp) || !aligned16(residual) || !aligned16(y)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(yp) || !aligned4(pos, w) || !aligned16(residual) || !aligned16(y)) return DG_ERR_ALIGNMENT;
     if (T == 0) return DG_OK;
     DeviceState* st = nullptr;
     if ((s = current_device(&st)) != DG_OK) return s;
@@ -941,7 +950,8 @@ dg_status dg_moe_combine_backward(const void* dy, const void* yp, const int32_t*
     int n16 = 0;
     dg_status s = check_rows(T, k, N, rows, dtype, m_indices, &n16);
     if (s != DG_OK) return s;
-    if (!aligned16(dy) || !aligned16(yp) || !aligned16(m_indices) || !aligned16(dyp)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(dy) || !aligned16(yp) || !aligned4(pos, w, dw) || !aligned16(m_indices) || !aligned16(dyp))
+        return DG_ERR_ALIGNMENT;
     if (T == 0) return DG_OK;
     // without weights every row's gradient is its token's: the dispatch of dy
     if (!w) return dg_moe_dispatch(dy, pos, m_indices, dyp, T, k, N, rows, dtype, stream);
@@ -959,7 +969,7 @@ dg_status dg_pack_sf_ue8m0(const float* sf, int32_t* out, int G, int MN, int K, 
     if (gran_mn != 1 && gran_mn != 128) return DG_ERR_INVALID_ARG;
     if (gran_k != 128) return DG_ERR_INVALID_ARG;
     if (K % 128 != 0) return DG_ERR_SHAPE;
-    if (!aligned16(out) || (reinterpret_cast<uintptr_t>(sf) & 3u)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(out) || !aligned4(sf)) return DG_ERR_ALIGNMENT;
     const int Kb = K / 128, Kp = (Kb + 3) / 4;
     if (Kp > 65535 || G > 65535) return DG_ERR_SHAPE;
     if (MN == 0) return DG_OK;
@@ -989,7 +999,7 @@ dg_status dg_pack_sf_ue8m0_k_grouped(const float* sf, int32_t* out, const int32_
                                      void* stream) {
     if (!ks || G <= 0 || MN < 0 || sum_K < 0 || (MN != 0 && sum_K != 0 && (!sf || !out))) return DG_ERR_INVALID_ARG;
     if (G > kMaxMaskedGroups || sum_K % 128 != 0) return DG_ERR_SHAPE;
-    if (!aligned16(out) || (reinterpret_cast<uintptr_t>(sf) & 3u)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(out) || !aligned4(sf, ks)) return DG_ERR_ALIGNMENT;
     const int kb_total = sum_K / 128;
     if (kb_total / 4 + G > 65535) return DG_ERR_SHAPE;
     if (MN == 0 || sum_K == 0) return DG_OK;

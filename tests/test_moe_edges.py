@@ -156,3 +156,23 @@ echo "$out" >> "$log"; touch "$out"
     (src / "two.cu").write_text("second")
     assert built() == {"two.o", "libdg.so.tmp", "dg_binding.so.tmp"}
     assert built() == set()
+
+
+def test_words_across_a_word_boundary_are_refused(lib):
+    # int32 and float32 tensors at an address that is no multiple of 4: a read of one would fault
+    half, align = ctypes.c_void_p(0x10002), 3
+    bad = [lib.dg_moe_sort(half, GOOD, GOOD, GOOD, None, 8, 2, 4, 512, None), lib.dg_moe_sort(GOOD, half, GOOD, GOOD, None, 8, 2, 4, 512, None),
+           lib.dg_moe_sort(GOOD, GOOD, GOOD, half, None, 8, 2, 4, 512, None), lib.dg_moe_sort(GOOD, GOOD, GOOD, GOOD, half, 8, 2, 4, 512, None),
+           lib.dg_moe_sort_masked(half, GOOD, GOOD, 8, 2, 4, 16, None), lib.dg_moe_sort_masked(GOOD, GOOD, half, 8, 2, 4, 16, None),
+           lib.dg_moe_dispatch(GOOD, half, None, GOOD, 8, 2, 256, 128, 0, None),
+           lib.dg_moe_dispatch_fp8(GOOD, half, None, GOOD, GOOD, 8, 2, 256, 1, 128, None),
+           lib.dg_moe_combine(GOOD, half, None, None, GOOD, 8, 2, 256, 128, 0, None),
+           lib.dg_moe_combine(GOOD, GOOD, half, None, GOOD, 8, 2, 256, 128, 0, None),
+           lib.dg_moe_combine_backward(GOOD, GOOD, GOOD, None, half, GOOD, GOOD, 8, 2, 256, 128, 0, None),
+           lib.dg_moe_combine_backward(GOOD, GOOD, GOOD, None, GOOD, GOOD, half, 8, 2, 256, 128, 0, None),
+           lib.dg_m_grouped_fp8_gemm_nt_contiguous_act(GOOD, GOOD, GOOD, GOOD, None, None, None, GOOD, half, 128, 512, 256, 4, 0, 0, None),
+           lib.dg_m_grouped_fp8_gemm_nt_masked_act(GOOD, GOOD, GOOD, GOOD, None, None, None, GOOD, half, 4, 64, 512, 256, 0, 0, None),
+           lib.dg_m_grouped_fp8_gemm_nt_contiguous(GOOD, GOOD, GOOD, GOOD, GOOD, half, 128, 512, 256, 4, None),
+           lib.dg_k_grouped_fp8_gemm_tn_contiguous(GOOD, GOOD, GOOD, GOOD, None, GOOD, half, 4, 64, 64, 128, None),
+           lib.dg_pack_sf_ue8m0_k_grouped(GOOD, GOOD, half, 4, 64, 128, None)]
+    assert bad == [align] * len(bad)
